@@ -420,8 +420,13 @@ __device__ __forceinline__ void arrive_remote(uint32_t local, uint32_t rank)
         : "memory");
 }
 
+// 1 once any wait of these kernels has run out (read and cleared by distill_status).
+__device__ unsigned wait_status;
+
+__device__ __forceinline__ void note_timeout() { atomicMax(&wait_status, kStatusWaitTimeout); }
+
 // Waits (bounded) for the arrivals of other blocks.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
     const uint64_t t0 = global_ns();
     for (uint32_t spins = 0; spins < (1u << 30); ++spins) {
@@ -434,7 +439,7 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity)
             : "r"(bar), "r"(parity)
             : "memory");
         if (ok) return true;
-        if (global_ns() - t0 > kWaitLimitNs) return false;
+        if (global_ns() - t0 > limit_ns) return false;
     }
     return false;
 }
@@ -452,7 +457,19 @@ __device__ __forceinline__ void data_barrier() { asm volatile("bar.sync 1, %0;" 
 // bytes that it has in global memory, -infinity in what is left of the first and last vector. The
 // list's tokens are taken out before the rest is summed; the blocks' sums go to every block of the
 // cluster, whose barriers in shared memory they arrive at. The logits are read once.
-template <typename IO, bool kGrad>
+//
+// Waits that run out. A block waits longer for the others' sums than they can wait for their copies,
+// so a copy that is late, or never lands, reaches the others as a sum (of NaN) and not as silence. A
+// warp whose copy has not landed starts no other, one that has waited for the cluster in vain exchanges
+// nothing more (its barriers' phases would no longer be the rows'): all its later rows are NaN.
+// The late block still writes to the others, so a warp that gave up does not end, and with
+// it its block's shared memory does not go, before every other warp of the cluster has ended or
+// given up as well; a block whose exchanges were all answered is written to no more.
+// kLate, for tests of that: the waits for the cluster end after kLateLimitNs, and the blocks of
+// rank 1 sleep for much longer before their first exchange.
+constexpr uint64_t kLateLimitNs = 2000000, kLateNs = 20 * kLateLimitNs;
+
+template <typename IO, bool kGrad, bool kLate>
 __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a, int blocks, int slice, int per)
 {
     constexpr int E = Vec<IO>::kN;
@@ -570,6 +587,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
     };
     if (!(weight_of(n) == 0.0f)) begin(n);
     uint32_t parity = 0, met = 0;
+    bool copied = true, joined = true;      // whether no wait of this warp has run out
     for (int turn = 0; n < a.N; n += step, turn ^= 1) {
         __syncthreads();                    // the list of this row is ready
         const Teacher t = list_of(turn);
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
         const List list = row.list;
         const float w = row.w;
         const bool live = !(w == 0.0f) && (a.top_lse || !(list.mass == 0.0f));
-        const bool next = n + step < a.N && !(row.next_w == 0.0f);      // whether there is a row to copy
+        bool next = n + step < a.N && !(row.next_w == 0.0f);        // whether there is a row to copy
         const IO* z = row_of(n) + v0;
         IO* d = kGrad ? static_cast<IO*>(a.dlogits) + n * a.ds + v0 : nullptr;
         const int phase = (int)phase_of(z, sizeof(IO));
@@ -589,11 +607,12 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
             at = (int)k;
             return t.first[j] >= 0 && k >= 0 && k < len && phase + k >= s0 * E && phase + k < s1 * E;
         };
-        bool fine = true;
-        if (!(w == 0.0f)) {
-            fine = mbar_wait(bar, parity) || mbar_wait(bar, parity);
+        if (!(w == 0.0f) && copied) {
+            copied = __all_sync(0xffffffffu, mbar_wait(bar, parity) || mbar_wait(bar, parity));
             parity ^= 1;
+            if (!copied) note_timeout();
         }
+        next = next && copied;
         RowGrad g{0.0f, 0.0f, 0.0f, 0.0f};
         float2 rest = make_float2(-INFINITY, 0.0f), all = rest;
         if (live) {
@@ -605,7 +624,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
             __syncwarp();
             rest = sum_vectors<IO>(buf, s0 + lane, 32, s1, k2);
             rest = warp_join(rest.x, rest.y, k2);
-            if (!fine) rest.y = __int_as_float(0x7fc00000);
+            if (!copied) rest.y = __int_as_float(0x7fc00000);
             if (lane == 0) part[turn][warp] = rest;
             if (!kGrad && next) {
                 fence_async();
@@ -615,19 +634,25 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
             data_barrier();
             rest = lane < kWarps ? part[turn][lane] : make_float2(-INFINITY, 0.0f);
             rest = warp_join(rest.x, rest.y, k2);
-            if (blocks > 1) {
+            if (blocks > 1 && joined) {
                 const int slot = met & 1;
+                if (kLate && met == 0 && rank == 1) {
+                    const uint64_t t0 = global_ns();
+                    for (int k = 0; k < 1000000 && global_ns() - t0 < kLateNs; ++k) __nanosleep(1000);
+                }
                 if (warp == 0 && lane < blocks) {
                     store_remote(smem_u32(&parts[slot][rank].x), (uint32_t)lane, rest.x);
                     store_remote(smem_u32(&parts[slot][rank].y), (uint32_t)lane, rest.y);
                     arrive_remote(smem_u32(&joins[slot]), (uint32_t)lane);
                 }
-                fine = wait_cluster(smem_u32(&joins[slot]), met >> 1 & 1);
+                constexpr uint64_t limit = kLate ? kLateLimitNs : 3 * kWaitLimitNs;
+                joined = __all_sync(0xffffffffu, wait_cluster(smem_u32(&joins[slot]), met >> 1 & 1, limit));
+                if (!joined) note_timeout();
                 ++met;
                 rest = lane < blocks ? parts[slot][lane] : make_float2(-INFINITY, 0.0f);
                 rest = warp_join(rest.x, rest.y, k2);
-                if (!fine) rest.y = __int_as_float(0x7fc00000);
             }
+            if (!joined) rest.y = __int_as_float(0x7fc00000);
             all = join(rest, make_float2(list.m, list.s), k2);
             g = row_grad(a, list, rest, all, k2);
         }
@@ -686,6 +711,11 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
                 if (a.stats) *reinterpret_cast<float4*>(a.stats + 4 * n) = make_float4(g.ref, g.inv, g.base, g.coef);
             }
         }
+    }
+    if (!joined) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();        // for the warps that have not ended; each of their waits is bounded
     }
 }
 
@@ -846,11 +876,11 @@ struct Resident {
     size_t smem = 0;
 };
 
-template <typename IO, bool kGrad>
+template <typename IO, bool kGrad, bool kLate = false>
 static cudaError_t run_row(const DistillArgs& a, const Plan& p, const DeviceFacts& dev, cudaStream_t s)
 {
     constexpr int E = Vec<IO>::kN;
-    constexpr auto kernel = k_distill_row<IO, kGrad>;
+    constexpr auto kernel = k_distill_row<IO, kGrad, kLate>;
     const int per = (p.slice / E + 1 + kWarps - 1) / kWarps;
     const size_t smem = (size_t)kWarps * per * 16 + (size_t)2 * padded(a.K) * kTeacherWords * 4;
     cudaLaunchConfig_t cfg{};
@@ -899,6 +929,25 @@ cudaError_t launch_distill(const DistillArgs& a, void* ws, cudaStream_t s)
         });
         return e != cudaSuccess || !b.dlogits ? e : launch_distill_bwd(b, s);
     });
+}
+
+cudaError_t launch_distill_late(const DistillArgs& a, cudaStream_t s)
+{
+    DeviceFacts dev;
+    const cudaError_t e = current_device(&dev);
+    if (e != cudaSuccess) return e;
+    const Plan p = plan_for(a.N, a.V, sizeof(float), dev.sms);
+    return p.blocks > 1 ? run_row<float, true, true>(a, p, dev, s) : cudaErrorInvalidValue;
+}
+
+cudaError_t distill_status(unsigned* status, cudaStream_t s)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(status, wait_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *status == 0u) return e;
+    static const unsigned zero = 0u;
+    e = cudaMemcpyToSymbolAsync(wait_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
 }
 
 cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t s)

@@ -96,5 +96,9 @@ cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t s);
 size_t distill_workspace_bytes(int64_t N, int64_t V, int dtype);
 cudaError_t launch_distill(const DistillArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t s);
+// Loss and gradient (float32) with one block of each cluster late, for tests.
+cudaError_t launch_distill_late(const DistillArgs& a, cudaStream_t s);
+// Synchronizes the stream; the kernels' status word of the current device, which it clears.
+cudaError_t distill_status(unsigned* status, cudaStream_t s);
 
 }  // namespace ob

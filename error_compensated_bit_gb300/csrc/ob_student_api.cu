@@ -167,6 +167,12 @@ int ob_gated_scan_read_status(const void* ws, unsigned* status, void* stream)
     return done(e);
 }
 
+int ob_operators_read_status(unsigned* status, void* stream)
+{
+    if (!status) return OB_EINVAL;
+    return done(distill_status(status, static_cast<cudaStream_t>(stream)));
+}
+
 size_t ob_distill_workspace_bytes(int64_t N, int64_t V, int dtype)
 {
     if (!dtype_ok(dtype) || N < 0 || V < 1) return 0;
@@ -231,6 +237,19 @@ int ob_distill_bwd(int64_t N, int64_t V, int64_t K, int dtype, const void* logit
     DistillArgs a{N, V, (int)K, dtype, index_bits, top_dtype, logits, zs, index, top, top_lse, weight, dloss,
                   1.0f / temperature, nullptr, dlogits, ds, const_cast<float*>(stats)};
     return done(launch_distill_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+int ob_selftest_distill_wait(int64_t N, int64_t V, int64_t K, const float* logits, const int64_t* index,
+                             const float* top, float* loss, float* dlogits, void* stream)
+{
+    OB_TRY(check_distill_sizes(N, V, K, OB_F32, 64, OB_F32, 1.0f));
+    if (N == 0 || V < 32768 || V > 131072) return OB_EINVAL;
+    OB_TRY(check_distill(N, V, K, OB_F32, logits, index, 64, top, OB_F32, nullptr, nullptr, 1.0f));
+    OB_TRY(want(loss, 4));
+    OB_TRY(want(dlogits, 4));
+    DistillArgs a{N, V, (int)K, OB_F32, 64, OB_F32, logits, V, index, top, nullptr, nullptr, nullptr,
+                  1.0f, loss, dlogits, V, nullptr};
+    return done(launch_distill_late(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -5,6 +5,7 @@ gradients that ``OneBitAdam`` and ``LocoAdam`` step with.
 ``gated_scan_step``    one token of it, for generation
 ``distill_loss``       the loss against a teacher's top logits, one value per row
 ``distill_loss_grad``  the same with the gradient by the logits, in one pass over them
+``read_status``        whether a kernel's bounded wait has run out since it was last asked
 
 Each is a call of the CUDA library (the contracts are in include/ob.h); ``gated_scan`` and
 ``distill_loss`` are differentiable by autograd. Work is enqueued on the current torch
@@ -69,6 +70,18 @@ def _call(device, name, *args):
             rc = _function(name)(*args, stream)
     if rc != ob.OB_OK:
         raise ob.ObError(name, rc)
+
+
+def read_status(device=None):
+    """Waits for the current stream of ``device`` (None: the current device), then reports and
+    clears its status: 0 when all the operators' kernels there have finished normally, 1 when one
+    has given up a wait (each is bounded, some seconds; what it wrote from there on is NaN)."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.index is None:
+        device = torch.device(device.type, torch.cuda.current_device())
+    status = ctypes.c_uint()
+    _call(device, "ob_operators_read_status", ctypes.byref(status))
+    return status.value
 
 
 def _view(t):

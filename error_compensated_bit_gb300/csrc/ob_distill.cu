@@ -940,15 +940,7 @@ cudaError_t launch_distill_late(const DistillArgs& a, cudaStream_t s)
     return p.blocks > 1 ? run_row<float, true, true>(a, p, dev, s) : cudaErrorInvalidValue;
 }
 
-cudaError_t distill_status(unsigned* status, cudaStream_t s)
-{
-    cudaError_t e = cudaMemcpyFromSymbolAsync(status, wait_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess || *status == 0u) return e;
-    static const unsigned zero = 0u;
-    e = cudaMemcpyToSymbolAsync(wait_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
-    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
-}
+cudaError_t distill_status(unsigned* status, cudaStream_t s) { return take_status(wait_status, status, s); }
 
 cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t s)
 {

@@ -776,6 +776,13 @@ __global__ void __launch_bounds__(256) k_clear(uint4* p, int64_t n)
         p[k] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// A look-back's wait for a slot that nothing publishes, for tests.
+__global__ void k_scan_wait(unsigned* header, uint64_t limit_ns)
+{
+    const Slot* slot = reinterpret_cast<const Slot*>(reinterpret_cast<char*>(header) + kScanHeader / 2);
+    await_slot(slot, kPartial, header, limit_ns);
+}
+
 // Bytes of slots for `steps`-step tiles, one tile an item: channels rounded up to the widest tile.
 size_t slot_bytes(int64_t B, int64_t T, int64_t D, int steps)
 {
@@ -936,5 +943,15 @@ cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t s)
         return cudaGetLastError();
     });
 }
+
+cudaError_t launch_scan_wait(void* ws, uint64_t limit_ns, cudaStream_t s)
+{
+    cudaError_t e = cudaMemsetAsync(ws, 0, kScanHeader, s);
+    if (e != cudaSuccess) return e;
+    k_scan_wait<<<1, 32, 0, s>>>(static_cast<unsigned*>(ws), limit_ns);
+    return cudaGetLastError();
+}
+
+cudaError_t scan_status(unsigned* status, cudaStream_t s) { return take_status(scan_wait_status, status, s); }
 
 }  // namespace ob

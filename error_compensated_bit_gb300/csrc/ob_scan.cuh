@@ -234,9 +234,12 @@ __device__ __forceinline__ void write_slot(Slot* p, float a, float h, unsigned f
         : "memory");
 }
 
-// Waits (bounded) until the slot holds at least `flag`. A wait that runs out sets the status
-// word and stands in a final NaN.
-__device__ __forceinline__ Slot await_slot(const Slot* p, unsigned flag, unsigned* status)
+// 1 once any wait of the scans has run out (read and cleared by scan_status).
+static __device__ unsigned scan_wait_status;
+
+// Waits (bounded) until the slot holds at least `flag`. A wait that runs out sets the workspace's
+// status word and the one above and stands in a final NaN.
+__device__ __forceinline__ Slot await_slot(const Slot* p, unsigned flag, unsigned* status, uint64_t limit_ns = kWaitLimitNs)
 {
     Slot s = read_slot(p);
     if (s.flag >= flag) return s;
@@ -244,9 +247,10 @@ __device__ __forceinline__ Slot await_slot(const Slot* p, unsigned flag, unsigne
     for (uint32_t spins = 0; spins < (1u << 30); ++spins) {
         s = read_slot(p);
         if (s.flag >= flag) return s;
-        if (global_ns() - t0 > kWaitLimitNs) break;
+        if (global_ns() - t0 > limit_ns) break;
     }
     atomicMax(status, kStatusWaitTimeout);
+    atomicMax(&scan_wait_status, kStatusWaitTimeout);
     return Slot{0.0f, __int_as_float(0x7fc00000), kFinal, 0u};
 }
 

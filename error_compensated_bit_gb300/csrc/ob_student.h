@@ -43,6 +43,18 @@ cudaError_t with_opt_in(int device, size_t most, F&& launch)
     return e;
 }
 
+// Synchronizes the stream; the value of a status word of the current device, which is cleared.
+template <typename Word>
+cudaError_t take_status(const Word& word, unsigned* status, cudaStream_t s)
+{
+    static const unsigned zero = 0u;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(status, word, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *status == 0u) return e;
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    return e != cudaSuccess ? e : cudaStreamSynchronize(s);
+}
+
 struct ScanArgs {
     int64_t B, T, D;
     int dtype;
@@ -92,13 +104,14 @@ size_t scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype, int back
 cudaError_t launch_scan_fwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs& a, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t s);
+cudaError_t launch_scan_wait(void* ws, uint64_t limit_ns, cudaStream_t s);     // a wait that runs out, for tests
+cudaError_t scan_status(unsigned* status, cudaStream_t s);
 
 size_t distill_workspace_bytes(int64_t N, int64_t V, int dtype);
 cudaError_t launch_distill(const DistillArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t s);
 // Loss and gradient (float32) with one block of each cluster late, for tests.
 cudaError_t launch_distill_late(const DistillArgs& a, cudaStream_t s);
-// Synchronizes the stream; the kernels' status word of the current device, which it clears.
 cudaError_t distill_status(unsigned* status, cudaStream_t s);
 
 }  // namespace ob

@@ -170,7 +170,19 @@ int ob_gated_scan_read_status(const void* ws, unsigned* status, void* stream)
 int ob_operators_read_status(unsigned* status, void* stream)
 {
     if (!status) return OB_EINVAL;
-    return done(distill_status(status, static_cast<cudaStream_t>(stream)));
+    unsigned scan = 0u, distill = 0u;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = scan_status(&scan, s);
+    if (e == cudaSuccess) e = distill_status(&distill, s);
+    if (e == cudaSuccess) *status = scan | distill;
+    return done(e);
+}
+
+int ob_selftest_scan_wait(void* ws, uint64_t limit_ns, void* stream)
+{
+    OB_TRY(want(ws, 256));
+    if (limit_ns < 1 || limit_ns > 2000000000ull) return OB_EINVAL;
+    return done(launch_scan_wait(ws, limit_ns, static_cast<cudaStream_t>(stream)));
 }
 
 size_t ob_distill_workspace_bytes(int64_t N, int64_t V, int dtype)

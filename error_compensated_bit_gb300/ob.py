@@ -70,6 +70,7 @@ SIGNATURES = {
     "ob_distill_bwd": (_int, [_i64, _i64, _i64, _int, _vp, _i64, _vp, _int, _vp, _int, _vp, _vp,
                               _f, _vp, _vp, _vp, _i64, _vp]),
     "ob_operators_read_status": (_int, [ctypes.POINTER(ctypes.c_uint), _vp]),
+    "ob_selftest_scan_wait": (_int, [_vp, ctypes.c_uint64, _vp]),
     "ob_selftest_distill_wait": (_int, [_i64, _i64, _i64] + [_vp] * 6),
 }
 

@@ -463,17 +463,21 @@ int ob_distill_bwd(int64_t N, int64_t V, int64_t K, int dtype, const void *logit
 /*
  * Synchronize the stream, then report and clear a status word of the operators above on the
  * current device: 0 when every call since the last read finished normally, 1 when a bounded wait
- * of one ran out (ob_distill: for a copy, 4 s, or for the other blocks of a row, 6 s; the
- * rows concerned, and those its blocks took after them, hold NaN).
+ * of one ran out (the scans: see ob_gated_scan_read_status; ob_distill: for a copy, 4 s, or for
+ * the other blocks of a row, 6 s; the rows concerned, and those its blocks took after them,
+ * hold NaN).
  */
 int ob_operators_read_status(unsigned *status, void *stream);
 
 /*
- * Self-test of that: ob_distill's pass over float32 logits [N][V] (32768 <= V <= 131072, so
+ * Self-tests of that. The scan's wait, for a state that nothing publishes: sets the status word of
+ * a scan workspace (256 bytes are enough, which it clears first) and the status above to 1 after
+ * limit_ns (1 .. 2e9) nanoseconds. And ob_distill's pass over float32 logits [N][V] (32768 <= V <= 131072, so
  * that several blocks share a row), with int64 indices, float32 top values and one block of
  * each row 40 ms late while the others wait 2 ms. Sets the status to 1; every loss and, outside
  * the late blocks' first rows, every gradient is NaN. Nothing faults and the device stays usable.
  */
+int ob_selftest_scan_wait(void *ws, uint64_t limit_ns, void *stream);
 int ob_selftest_distill_wait(int64_t N, int64_t V, int64_t K, const float *logits,
                              const int64_t *index, const float *top, float *loss, float *dlogits,
                              void *stream);

@@ -34,6 +34,23 @@ def test_a_late_block_of_a_row_is_reported(ops, N, V):
     assert ops.read_status(z.device) == 0
 
 
+def test_a_scan_s_wait_is_reported(ops):
+    import ctypes
+    from error_compensated_bit_gb300 import ob
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    assert ops.read_status() == 0
+    ops._call(ws.device, "ob_selftest_scan_wait", ws.data_ptr(), 2_000_000)
+    st = ctypes.c_uint(9)
+    ops._call(ws.device, "ob_gated_scan_read_status", ws.data_ptr(), ctypes.byref(st))
+    assert st.value == 1 and ops.read_status() == 1 and ops.read_status() == 0
+    x = torch.ones(1, 1000, 64, device="cuda")
+    y, _ = ops.gated_scan(x, x, x, torch.ones(64, device="cuda"))
+    assert bool(torch.isfinite(y).all()) and ops.read_status() == 0
+    assert ob.load().ob_selftest_scan_wait(ws.data_ptr(), 0, None) == ob.OB_EINVAL
+    assert ob.load().ob_selftest_scan_wait(ws.data_ptr(), 3 * 10 ** 9, None) == ob.OB_EINVAL
+    assert ob.load().ob_selftest_scan_wait(ws.data_ptr() + 4, 1000, None) == ob.OB_EALIGN
+
+
 def test_refusals(ops):
     from error_compensated_bit_gb300 import ob
     lib, good = ob.load(), 1 << 20

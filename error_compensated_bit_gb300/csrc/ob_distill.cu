@@ -3,9 +3,10 @@
 // With z' = z/tau, lse the log-sum-exp of a row's z' and rest the one over the tokens
 // outside the teacher's list, the loss is
 //   sum_j p_j log p_j - sum_j p_j (z'_j - lse)  [+ p_rest (log p_rest - (rest - lse))]
-// and its gradient by z, times tau:
-//   q_v - p_v on the list, softmax_rest(z')_v * (q_rest - p_rest) outside it,
-// q_rest = exp(rest - lse), p_rest = 0 without a rest entry. Summing the rest apart (rather
+// and its gradient by z, times tau, with M = sum_j p_j + p_rest:
+//   M q_v - p_v on the list, softmax_rest(z')_v * (M q_rest - p_rest) outside it,
+// q_rest = exp(rest - lse), p_rest = 0 without a rest entry. M is 1 unless the list's own mass is
+// above 1 (top values rounded to 16 bits beside the log-sum-exp of the unrounded ones): p_rest is 0 there. Summing the rest apart (rather
 // than as 1 minus the list) keeps its precision when the list holds nearly all the mass.
 //
 // What has to move: each logit in once and, with the gradient, out once; the lists are small. The
@@ -222,7 +223,7 @@ __device__ __forceinline__ List read_list(const DistillArgs& a, int64_t n, const
     return *shared;
 }
 
-// What a row's gradient is made of: q = 2^(z*k2 - ref) * inv on the list, and (q_rest - p_rest) times
+// What a row's gradient is made of: M q = 2^(z*k2 - ref) * inv on the list, and (M q_rest - p_rest) times
 // the softmax of the rest, 2^(z*k2 - base) * coef, outside it. inv is 0 for a row without a loss.
 struct RowGrad {
     float ref, inv, base, coef;
@@ -233,7 +234,7 @@ __device__ __forceinline__ RowGrad row_grad(const DistillArgs& a, const List& l,
     const float prest = a.top_lse ? fmaxf(0.0f, 1.0f - l.mass) : 0.0f;
     RowGrad g;
     g.ref = all.x == -INFINITY ? 0.0f : ref(all.x, k2);
-    g.inv = __fdividef(1.0f, all.y);
+    g.inv = __fdividef(a.top_lse && !(l.mass <= 1.0f) ? l.mass : 1.0f, all.y);
     const bool none = rest.y == 0.0f;
     g.base = none ? 0.0f : ref(rest.x, k2);
     g.coef = none ? 0.0f : fast_exp2(g.base - g.ref) * g.inv - __fdividef(prest, rest.y);

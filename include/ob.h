@@ -438,7 +438,9 @@ int ob_gated_scan_read_status(const void *ws, unsigned *status, void *stream);
  * weight is 0, or (without top_lse) with no entry above -infinity, has loss 0 and gradient 0,
  * whatever its logits are. weight [N] (NULL: 1) multiplies the loss.
  * loss [N] is written; dlogits (NULL: not wanted) [N][V], row stride ds, receives the gradient
- * of sum(loss), weight/temperature*(q - p) in its general form, in the same pass; it may be
+ * of sum(loss) in the same pass: weight/temperature*(M*q - p) on the list and
+ * weight/temperature*(M*q_rest - p_rest)*(the softmax of the tokens outside) elsewhere, with
+ * M = sum p + p_rest, which is 1 but where rounded top values sum to more than 1. It may be
  * logits itself (same stride) but must not otherwise overlap it. stats (NULL: not wanted)
  * [N][4] receives what ob_distill_bwd needs (16-byte aligned). ws: ob_distill_workspace_bytes(...) bytes
  * (may be 0, ws then may be NULL). K 0 .. OB_DISTILL_MAX_K, V >= 1, N may be 0;

@@ -54,6 +54,7 @@ __device__ __forceinline__ Teacher teacher_at(void* base, int K)
 // What a row's list comes to.
 struct List {
     float self, mass;           // sums of p log p, p
+    float rest, slack;          // p_rest, and how much of it the roundings of mass may have made
     float m, s;                 // its student logits' sum of exponentials, as below
 };
 
@@ -160,7 +161,7 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
         for (int j = lane; j < K; j += 32) sum += t.t[j] == -INFINITY ? 0.0f : expf(t.t[j] - top);
         lse = top + logf(warp_sum(sum));
     }
-    List l{0.0f, 0.0f, m, 0.0f};
+    List l{0.0f, 0.0f, 0.0f, 0.0f, m, 0.0f};
     for (int j0 = 0; j0 < K; j0 += 32) {
         const int j = j0 + lane, k = j < K ? t.token[j] : -1;
         bool taken = false;
@@ -204,7 +205,20 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
     l.s = warp_sum(l.s);
     l.self = warp_sum(l.self);
     l.mass = warp_sum(l.mass);
+    if (a.top_lse) {
+        l.rest = fmaxf(0.0f, 1.0f - l.mass);
+        // an entry that counts has top/tau near lse: two roundings of the one, one of the other, one of their
+        // difference, the exponential's 4; and the sum's
+        l.slack = 0x1p-24f * (4.0f * fabsf(lse) + (float)K / 32.0f + 16.0f);
+    }
     return l;
+}
+
+// p_rest. Where the student has no mass outside the list any of it makes the loss infinite, so there
+// what rounding may have left does not count.
+__device__ __forceinline__ float rest_mass(const List& l, float2 rest)
+{
+    return rest.y == 0.0f && l.rest <= l.slack ? 0.0f : l.rest;
 }
 
 // The same for a whole block: warp 0 prepares the list of row n (z: the whole row) and tells the
@@ -231,10 +245,10 @@ struct RowGrad {
 
 __device__ __forceinline__ RowGrad row_grad(const DistillArgs& a, const List& l, float2 rest, float2 all, float k2)
 {
-    const float prest = a.top_lse ? fmaxf(0.0f, 1.0f - l.mass) : 0.0f;
+    const float prest = rest_mass(l, rest);
     RowGrad g;
     g.ref = all.x == -INFINITY ? 0.0f : ref(all.x, k2);
-    g.inv = __fdividef(a.top_lse && !(l.mass <= 1.0f) ? l.mass : 1.0f, all.y);
+    g.inv = __fdividef(a.top_lse && prest == 0.0f ? l.mass : 1.0f, all.y);     // mass + prest
     const bool none = rest.y == 0.0f;
     g.base = none ? 0.0f : ref(rest.x, k2);
     g.coef = none ? 0.0f : fast_exp2(g.base - g.ref) * g.inv - __fdividef(prest, rest.y);
@@ -253,7 +267,7 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t
     cross = warp_sum(cross) * a.inv_tau;
     float loss = l.self;
     if (!(l.mass == 0.0f)) loss -= cross - l.mass * over;
-    const float prest = a.top_lse ? fmaxf(0.0f, 1.0f - l.mass) : 0.0f;
+    const float prest = rest_mass(l, rest);
     if (prest > 0.0f) {
         const float lrest = rest.y == 0.0f ? -INFINITY : (rest.x - all.x) * a.inv_tau + log_over(rest, k2);
         loss += prest * (logf(prest) - (lrest - over));

@@ -290,7 +290,8 @@ def distill_loss(logits, index, top, top_lse=None, temperature=1.0, weight=None)
     teacher sent; entries with an index outside [0, V) are padding. Without ``top_lse`` the
     teacher is the softmax of those values / temperature. With it ([...] float32, the
     log-sum-exp of all the teacher's logits / temperature) the tokens outside the list are
-    one more entry, with the mass that both sides have left there. ``weight`` [...] float32
+    one more entry, with the mass that both sides have left there (a student without any has an
+    infinite loss, unless the teacher's is within rounding of 0). ``weight`` [...] float32
     multiplies the loss; rows of weight 0 (padding) and, without ``top_lse``, rows without an
     entry give 0. Differentiable by logits. Reduce it as the training loop wants; where the
     gradient's row factors are known beforehand, ``distill_loss_grad`` reads the logits once

@@ -2,8 +2,8 @@
 
 Plain torch in double precision on the CPU, from the formulas in include/ob.h: the gradient is
 the loss's derivative also where the listed mass S = sum p exceeds 1 (p_rest is 0 there, and the
-student's q counts S times), and there is no rest entry where the list holds the whole vocabulary
-or where the student has no mass outside it and p_rest is within a sum's rounding.
+student's q counts S times), and where the student has no mass outside the list a p_rest within a sum's
+rounding is 0.
 
 Logits are taken relative to their row's largest, dz <= 0, which leaves q and the loss as they
 are. EPS is float32's unit roundoff. An exponent dz is formed with at most 4 roundings of its own
@@ -74,7 +74,7 @@ def distill(logits, index, top, top_lse=None, temperature=1.0, weight=None, dlos
         lrest = torch.logsumexp(outside, 0)
         mass, emass = p.sum(), ep.sum() + C * p.sum() + 4 * EPS
         rest = torch.zeros((), dtype=torch.float64)
-        if top_lse is not None and not bool(listed.all()):
+        if top_lse is not None:
             rest = torch.clamp(1 - mass, min=0)
             if lrest == -INF and rest <= rest_slack(float(tl), K):
                 rest = torch.zeros_like(rest)

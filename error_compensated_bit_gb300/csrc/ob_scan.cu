@@ -275,6 +275,15 @@ __device__ __forceinline__ float2 product(const float2* a, unsigned resets)
     return resets ? both(0.0f) : A;
 }
 
+// The decay over two stretches of steps. Where there can be resets a 0 wins, even over the NaN that a NaN
+// gate makes: nothing from before a reset passes it.
+__device__ __forceinline__ float2 both_decays(float2 a, float2 b, bool can_reset)
+{
+    const float2 p = mul2(a, b);
+    if (!can_reset) return p;
+    return make_float2(a.x == 0.0f || b.x == 0.0f ? 0.0f : p.x, a.y == 0.0f || b.y == 0.0f ? 0.0f : p.y);
+}
+
 // a*h + u; where there can be resets a 0 drops h, even an infinite one.
 __device__ __forceinline__ float2 join(float2 a, float2 h, float2 u, bool can_reset)
 {
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_fwd(ScanArgs p, Grid
             for (int e = 1; e < kWarps; ++e) {
                 const float2 aw = sa[turn][e][lane];
                 tH = join(aw, tH, sh[turn][e][lane], can_reset);
-                tA = mul2(tA, aw);
+                tA = both_decays(tA, aw, can_reset);
             }
         }
         // what the next tile of the chain waits for goes out before the copies of this block's next start
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_bwd(ScanArgs p, floa
             for (int e = kWarps - 2; e >= 0; --e) {
                 const float2 aw = sa[turn][e][lane];
                 tF = join(aw, tF, sf[turn][e][lane], can_reset);
-                tA = mul2(tA, aw);
+                tA = both_decays(tA, aw, can_reset);
             }
         }
         constexpr bool kEarly = V == 1;      // as in the forward pass

@@ -288,7 +288,7 @@ __device__ void look_back(const Slot* prev, int64_t stride, int pos, float2* win
     for (int v = 0; v < V; ++v) {
         const float2* w = win + lane * V + v;
         int k = 0;
-        while (k < rows - 1 && w[k * 32 * V].x >= 0.0f) ++k;
+        while (k < rows - 1 && !(w[k * 32 * V].x < 0.0f)) ++k;     // a NaN is no final entry
         float c = w[k * 32 * V].y;
         for (--k; k >= 0; --k) c = carry_on(w[k * 32 * V].x, c, w[k * 32 * V].y);
         carry[v] = c;

@@ -264,7 +264,7 @@ __device__ __forceinline__ float2 end_flow(const float2* a, const unsigned* wd, 
     return f;
 }
 
-// The product of a lane's L decays (0 with a reset among them).
+// The product of a lane's L decays (kResetDecay with a reset among them, which all channels of a row share).
 template <int V, int L>
 __device__ __forceinline__ float2 product(const float2* a, unsigned resets)
 {
@@ -272,23 +272,25 @@ __device__ __forceinline__ float2 product(const float2* a, unsigned resets)
 #pragma unroll
     for (int m = 0; m < L * V / 2; ++m) A = mul2(A, a[m]);
     if (V == 1) A.x *= A.y;
-    return resets ? both(0.0f) : A;
+    return resets ? both(kResetDecay) : A;
 }
 
-// The decay over two stretches of steps. Where there can be resets a 0 wins, even over the NaN that a NaN
-// gate makes: nothing from before a reset passes it.
+// The decay over two stretches of steps. A reset in either wins, even over the NaN that a NaN gate makes.
 __device__ __forceinline__ float2 both_decays(float2 a, float2 b, bool can_reset)
 {
     const float2 p = mul2(a, b);
     if (!can_reset) return p;
-    return make_float2(a.x == 0.0f || b.x == 0.0f ? 0.0f : p.x, a.y == 0.0f || b.y == 0.0f ? 0.0f : p.y);
+    const bool r = is_reset(a.x) || is_reset(b.x);
+    return make_float2(r ? kResetDecay : p.x, r ? kResetDecay : p.y);
 }
 
-// a*h + u; where there can be resets a 0 drops h, even an infinite one.
+// a*h + u, without a*h where a reset is among the steps of a.
 __device__ __forceinline__ float2 join(float2 a, float2 h, float2 u, bool can_reset)
 {
-    if (!can_reset) return fma2(a, h, u);
-    return make_float2(carry_on(a.x, h.x, u.x), carry_on(a.y, h.y, u.y));
+    const float2 n = fma2(a, h, u);
+    if (!can_reset) return n;
+    const bool r = is_reset(a.x);
+    return make_float2(r ? u.x : n.x, r ? u.y : n.y);
 }
 
 // The state that reaches an item, where it is known at once: the initial one for a chain's first, or
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_fwd(ScanArgs p, Grid
             // every warp has read its words of this tile: their place serves the look-back
             static_assert(kWarps * kWords * 4 >= kWindow * S::kCols * 8, "room for the look-back");
             float2* win = reinterpret_cast<float2*>(words + turn * kWarps * kWords);
-            look_back<V, kWarps>(mine - stride, stride, divide(q.item, g.by_chains), win, carry, header);
+            look_back<V, kWarps, kReset>(mine - stride, stride, divide(q.item, g.by_chains), win, carry, header);
         }
         if (!kEarly || !all_known) hand_on();
 #pragma unroll
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_bwd(ScanArgs p, floa
         sum_part(turn ^ 1);
         if (!all_known) {
             if (!kEarly && partial) publish<V>(mine, tA, tF, kPartial);
-            look_back<V, kWarps>(mine - stride, stride, divide(q.item, g.by_chains), win, carry, header);
+            look_back<V, kWarps, kReset>(mine - stride, stride, divide(q.item, g.by_chains), win, carry, header);
         }
         if (!kEarly || !all_known) hand_on();
 #pragma unroll

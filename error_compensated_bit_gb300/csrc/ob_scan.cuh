@@ -127,8 +127,11 @@ __device__ __forceinline__ Gates gates(float2 r, float2 i, const Rate& k, const 
     return g;
 }
 
-// a*h + u where a = 0 drops h, whatever it is (a reset drops even an infinite state).
-__device__ __forceinline__ float carry_on(float a, float h, float u) { return a == 0.0f ? u : fmaf(a, h, u); }
+// The decay over steps with a reset among them, which drops whatever state came before, even an
+// infinite one or a NaN. Decays and their products are never -0, and one that is small enough to have become +0
+// is no reset: an infinite state or a NaN goes on through it.
+constexpr float kResetDecay = -0.0f;
+__device__ __forceinline__ bool is_reset(float a) { return __float_as_uint(a) == 0x80000000u; }
 
 // ---- a lane's elements ----------------------------------------------------------------------------
 //
@@ -258,7 +261,7 @@ __device__ __forceinline__ Slot await_slot(const Slot* p, unsigned flag, unsigne
 // before are at `prev`, those of earlier ones `stride` slots lower each). All kWarps warps of the
 // block call it; lane l has channels l*V .. l*V+V-1. win: [kWindow][32*V] in shared memory; an
 // entry's A is -1 where it is final.
-template <int V, int kWarps>
+template <int V, int kWarps, bool kReset>
 __device__ void look_back(const Slot* prev, int64_t stride, int pos, float2* win, float carry[V], unsigned* status)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -290,7 +293,10 @@ __device__ void look_back(const Slot* prev, int64_t stride, int pos, float2* win
         int k = 0;
         while (k < rows - 1 && !(w[k * 32 * V].x < 0.0f)) ++k;     // a NaN is no final entry
         float c = w[k * 32 * V].y;
-        for (--k; k >= 0; --k) c = carry_on(w[k * 32 * V].x, c, w[k * 32 * V].y);
+        for (--k; k >= 0; --k) {
+            const float2 e = w[k * 32 * V];
+            c = kReset && is_reset(e.x) ? e.y : fmaf(e.x, c, e.y);
+        }
         carry[v] = c;
     }
 }

@@ -1,4 +1,6 @@
-"""What crosses a reset in the gated scan: nothing, a NaN gate included, forward and backward."""
+"""What crosses a reset in the gated scan: nothing, a NaN gate included, forward and backward; and
+what does not stop at one that is not there: infinities and NaN travel on however small the
+decays' product becomes, the same way in every run."""
 import pytest
 import torch
 
@@ -7,7 +9,7 @@ from test_gpu_scan import forward_backward, inputs, ops  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
-NAN = float("nan")
+INF, NAN = float("inf"), float("nan")
 
 # one-tile items of few chains; whole chains a block (on 152 SMs); runs of tiles; single channels
 SHAPES = [(2, 700, 66, F32), (3, 700, 130, BF16), (2, 700, 33, F16), (5, 300, 3200, BF16), (20, 700, 1024, BF16),
@@ -60,3 +62,40 @@ def test_nan_gates_everywhere_but_in_one_sequence(ops, B, T, D, dtype):  # noqa:
     for name in ("y", "dx", "dr", "di"):
         assert torch.equal(bad[name][:, 150:290], clean[name][:, 150:290]), name
     assert bool(torch.isnan(bad["y"][:, :150]).all()) and bool(torch.isnan(bad["h"]).all())
+
+
+@pytest.mark.parametrize("B,T,D,dtype", [(1, 4000, 66, F32), (2, 4000, 70, BF16), (1, 4000, 33, F16),
+                                         (20, 900, 1024, BF16), (5, 900, 3200, BF16)])
+@pytest.mark.parametrize("resets", [False, True])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_what_is_not_finite_stays(ops, B, T, D, dtype, resets, value):  # noqa: F811
+    """Decays whose product over a tile is far below the smallest float32: no state is dropped by
+    it, whether the row has a reset before (or after) or the batch has no flags at all."""
+    k = inputs(B, T, D, dtype, seed=32, state=True, grads=True)
+    k["decay"][:] = 6.0
+    at, far = 300, T - 200
+    if resets:
+        k["reset"] = torch.zeros(B, T, dtype=torch.bool, device="cuda")
+        k["reset"][:, [77, far + 100]] = True
+    clean = forward_backward(ops, k)
+    q = dict(k, x=k["x"].clone(), dy=k["dy"].clone())
+    q["x"][:, at, ::3] = value
+    q["dy"][:, far, 1::3] = value
+    first = forward_backward(ops, q)
+    end = far + 100 if resets else T
+    hurt = torch.zeros(B, T, D, dtype=torch.bool, device="cuda")
+    hurt[:, at:end, ::3] = True
+    assert not torch.isfinite(first["y"][hurt]).any()
+    assert torch.equal(first["y"][~hurt], clean["y"][~hurt])
+    back = torch.zeros(B, T, D, dtype=torch.bool, device="cuda")
+    back[:, 77 if resets else 0:far + 1, 1::3] = True
+    assert not torch.isfinite(first["dx"][back]).any()
+    if resets:
+        assert torch.equal(first["dx"][~back & ~hurt], clean["dx"][~back & ~hurt]) and torch.equal(first["dh0"], clean["dh0"])
+    else:
+        assert not torch.isfinite(first["dh0"][:, 1::3]).any()
+    for _ in range(6):
+        again = forward_backward(ops, q)
+        for name in first:
+            a, b = first[name], again[name]
+            assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)), name

@@ -97,7 +97,8 @@ __device__ __forceinline__ float2 logistic32(float2 v, const Held& c)
         float2 e = fma2(v, c.half_log2e, make_float2(-m.x, -m.y));
         e = fma2(v, both(lo), e);
         e = make_float2(fminf(e.x, 1.0f), fminf(e.y, 1.0f));     // NaN, from an infinite v, becomes 1
-        n = fma2(n, mul2(e, both(0.6931471805599453f)), n);
+        // a factor that is finite and not 0, so that an overflown n stays infinite (of either sign: it is squared)
+        n = mul2(n, fma2(e, both(0.6931471805599453f), both(1.0f)));
     }
     const float2 d = fma2(mul2(n, c.two_m32), n, c.two_m32);
     return make_float2(fast_rcp(d.x), fast_rcp(d.y));

@@ -95,33 +95,54 @@ __device__ __forceinline__ int token_at(const DistillArgs& a, int64_t o)
 // (m, s) stands for s * 2^c(m), c(m) = m*k2 rounded to float32 and k2 = log2(e)/tau: s is the sum over
 // some logits z of 2^(z*k2 - c), each exponent formed by one multiply-add, so that the rounding of c
 // (of the order of 1e-6) is the same in every term and in what is made of s later, and drops out.
+//
+// That rounding grows with m and would overflow the terms themselves (a row at -1e30 or at the type's
+// lowest value). From |m*k2| = kHuge on c(m) is m*k2 itself: any two float32 values of which one is
+// that large are at least 64 apart in z*k2, so the terms are 1 where z = m and nothing to float32
+// elsewhere, which a power of two in place of k2 makes exactly.
 
-// c(m). The type's lowest values, used as masks, stay finite.
-__device__ __forceinline__ float ref(float m, float k2)
+constexpr float kHuge = 1073741824.0f;      // 2^30
+
+// The exponent of a logit z <= m is z*k - c.
+struct Scale {
+    float k, c;
+};
+
+__device__ __forceinline__ Scale scale_of(float m, float k2)
 {
-    const float v = m * k2;
-    return v == -INFINITY && m != -INFINITY ? -3.4028235e38f : v;
+    const float c = m * k2;
+    if (fabsf(c) < kHuge) return Scale{k2, c};
+    if (isinf(m)) return Scale{k2, fmaxf(m, 0.0f)};
+    // k*|m| in [2^30, 2^31)
+    const unsigned e = __float_as_uint(m) >> 23 & 255u;
+    const float k = __uint_as_float(min(284u - e, 254u) << 23);
+    return Scale{k, k * m};
+}
+
+// 2^(c(a) - c(b)) for a <= b.
+__device__ __forceinline__ float between(float a, float b, float k2)
+{
+    const float ca = a * k2, cb = b * k2, f = fast_exp2(ca - cb);
+    return a == b ? 1.0f : fmaxf(fabsf(ca), fabsf(cb)) < kHuge ? f : 0.0f;
 }
 
 __device__ __forceinline__ float2 join(float2 a, float2 b, float k2)
 {
-    if (a.x == -INFINITY && b.x == -INFINITY) return make_float2(a.x, a.y + b.y);
-    const float m = fmaxf(a.x, b.x), c = ref(m, k2);
-    return make_float2(m, a.y * fast_exp2(ref(a.x, k2) - c) + b.y * fast_exp2(ref(b.x, k2) - c));
+    const float m = fmaxf(a.x, b.x);
+    return make_float2(m, a.y * between(a.x, m, k2) + b.y * between(b.x, m, k2));
 }
 
 // (m, s) of every lane joined, in every lane. An empty one is (-infinity, 0); a sum of NaN stays.
 __device__ __forceinline__ float2 warp_join(float m, float s, float k2)
 {
     const float top = warp_max(m);
-    if (top == -INFINITY) return make_float2(top, warp_sum(s));
-    return make_float2(top, warp_sum(s * fast_exp2(ref(m, k2) - ref(top, k2))));
+    return make_float2(top, warp_sum(s * between(m, top, k2)));
 }
 
 // log(s * 2^c(m)) - m/tau: what the rounding of c makes of log(s).
 __device__ __forceinline__ float log_over(float2 a, float k2)
 {
-    const float c = ref(a.x, k2), off = a.x * k2 == -INFINITY ? 0.0f : kLn2 * fmaf(-a.x, k2, c);
+    const float c = a.x * k2, off = fabsf(c) < kHuge ? kLn2 * fmaf(-a.x, k2, c) : 0.0f;
     return a.y == 0.0f ? -INFINITY : logf(a.y) + off;
 }
 
@@ -199,9 +220,9 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
             __syncwarp();
         }
     }
-    const float c = m == -INFINITY ? 0.0f : ref(m, k2);
+    const Scale c = scale_of(m, k2);
     for (int j = lane; j < K; j += 32)
-        if (t.first[j] >= 0) l.s += fast_exp2(fmaf(t.z[j], k2, -c));
+        if (t.first[j] >= 0) l.s += fast_exp2(fmaf(t.z[j], c.k, -c.c));
     l.s = warp_sum(l.s);
     l.self = warp_sum(l.self);
     l.mass = warp_sum(l.mass);
@@ -214,11 +235,12 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
     return l;
 }
 
-// p_rest. Where the student has no mass outside the list any of it makes the loss infinite, so there
-// what rounding may have left does not count.
-__device__ __forceinline__ float rest_mass(const List& l, float2 rest)
+// p_rest. Where the student has no mass outside the list (its logits there are masked, by -infinity or a
+// value so far below the largest that float32 has no ratio for it) any of it makes the loss huge or
+// infinite, so there what rounding may have left does not count.
+__device__ __forceinline__ float rest_mass(const List& l, float2 rest, float2 all, float k2)
 {
-    return rest.y == 0.0f && l.rest <= l.slack ? 0.0f : l.rest;
+    return l.rest <= l.slack && between(rest.x, all.x, k2) == 0.0f ? 0.0f : l.rest;
 }
 
 // The same for a whole block: warp 0 prepares the list of row n (z: the whole row) and tells the
@@ -237,21 +259,21 @@ __device__ __forceinline__ List read_list(const DistillArgs& a, int64_t n, const
     return *shared;
 }
 
-// What a row's gradient is made of: M q = 2^(z*k2 - ref) * inv on the list, and (M q_rest - p_rest) times
-// the softmax of the rest, 2^(z*k2 - base) * coef, outside it. inv is 0 for a row without a loss.
+// What a row's gradient is made of: M q = 2^(z*k2 - c(top)) * inv on the list, and (M q_rest - p_rest) times
+// the softmax of the rest, 2^(z*k2 - c(rest)) * coef, outside it; top and rest are the largest logits.
+// inv is 0 for a row without a loss.
 struct RowGrad {
-    float ref, inv, base, coef;
+    float top, inv, rest, coef;
 };
 
 __device__ __forceinline__ RowGrad row_grad(const DistillArgs& a, const List& l, float2 rest, float2 all, float k2)
 {
-    const float prest = rest_mass(l, rest);
+    const float prest = rest_mass(l, rest, all, k2);
     RowGrad g;
-    g.ref = all.x == -INFINITY ? 0.0f : ref(all.x, k2);
+    g.top = all.x;
     g.inv = __fdividef(a.top_lse && prest == 0.0f ? l.mass : 1.0f, all.y);     // mass + prest
-    const bool none = rest.y == 0.0f;
-    g.base = none ? 0.0f : ref(rest.x, k2);
-    g.coef = none ? 0.0f : fast_exp2(g.base - g.ref) * g.inv - __fdividef(prest, rest.y);
+    g.rest = rest.x;
+    g.coef = rest.y == 0.0f ? 0.0f : between(rest.x, all.x, k2) * g.inv - __fdividef(prest, rest.y);
     return g;
 }
 
@@ -267,7 +289,7 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t
     cross = warp_sum(cross) * a.inv_tau;
     float loss = l.self;
     if (!(l.mass == 0.0f)) loss -= cross - l.mass * over;
-    const float prest = rest_mass(l, rest);
+    const float prest = rest_mass(l, rest, all, k2);
     if (prest > 0.0f) {
         const float lrest = rest.y == 0.0f ? -INFINITY : (rest.x - all.x) * a.inv_tau + log_over(rest, k2);
         loss += prest * (logf(prest) - (lrest - over));
@@ -373,8 +395,9 @@ __device__ __forceinline__ float2 sum_vectors(const IO* buf, int from, int step,
     VecMax<IO> top;
 #pragma unroll 4
     for (int k = from; k < end; k += step) top.add(load_vec<IO>(buf + k * E));
-    const float m = top.get(), c = m == -INFINITY ? 0.0f : ref(m, k2);
-    const float2 kk = hold(k2), cc = both(-c);
+    const float m = top.get();
+    const Scale c = scale_of(m, k2);
+    const float2 kk = hold(c.k), cc = both(-c.c);
     float2 s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll 4
     for (int k = from; k < end; k += step) {
@@ -390,13 +413,13 @@ __device__ __forceinline__ float2 sum_vectors(const IO* buf, int from, int step,
     return make_float2(m, s0.x + s0.y);
 }
 
-// coef * 2^(z k2 - base) of a vector.
+// coef * 2^(z kk - c) of a vector.
 template <typename IO>
-__device__ __forceinline__ void grad_vector(Vec<IO>& v, float2 kk, float2 minus_base, float2 coef)
+__device__ __forceinline__ void grad_vector(Vec<IO>& v, float2 kk, float2 minus_c, float2 coef)
 {
 #pragma unroll
     for (int e = 0; e < Vec<IO>::kN; e += 2) {
-        const float2 p = fma2(two(v, e), kk, minus_base);
+        const float2 p = fma2(two(v, e), kk, minus_c);
         set_two(v, e, mul2(coef, make_float2(fast_exp2(p.x), fast_exp2(p.y))));
     }
 }
@@ -673,17 +696,18 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
         }
         if (kGrad) {
             const float f = w * a.inv_tau, coef = f * g.coef;
+            const Scale c = scale_of(g.rest, k2);
             auto grad = [&](int at) {
-                return live ? from_f32<IO>(coef * fast_exp2(fmaf(to_f32(buf[phase + at]), k2, -g.base))) : from_f32<IO>(0.0f);
+                return live ? from_f32<IO>(coef * fast_exp2(fmaf(to_f32(buf[phase + at]), c.k, -c.c))) : from_f32<IO>(0.0f);
             };
             if (phase_of(d, sizeof(IO)) == (uint32_t)phase) {
-                const float2 kk = hold(k2), mb = hold(-g.base), cc = hold(coef);
+                const float2 kk = hold(c.k), mc = hold(-c.c), cc = hold(coef);
                 IO* o = d - phase;
                 if (live) {
 #pragma unroll 4
                     for (int k = lo + lane; k < hi; k += 32) {
                         Vec<IO> v = load_vec<IO>(buf + k * E);
-                        grad_vector(v, kk, mb, cc);
+                        grad_vector(v, kk, mc, cc);
                         store_vec(o + k * E, v);
                     }
                 } else {
@@ -709,9 +733,10 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
             }
             __syncwarp();
             if (live) {
+                const Scale top = scale_of(g.top, k2);
                 for (int j = lane; j < a.K; j += 32) {
                     int at;
-                    if (mine(j, at)) d[at] = from_f32<IO>(f * (fast_exp2(fmaf(t.z[j], k2, -g.ref)) * g.inv - t.total[j]));
+                    if (mine(j, at)) d[at] = from_f32<IO>(f * (fast_exp2(fmaf(t.z[j], top.k, -top.c)) * g.inv - t.total[j]));
                 }
             }
         } else if (!live && next) {
@@ -723,7 +748,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
             const float loss = live ? w * row_loss(a, t, list, rest, all, k2) : 0.0f;
             if (lane == 0) {
                 a.loss[n] = loss;
-                if (a.stats) *reinterpret_cast<float4*>(a.stats + 4 * n) = make_float4(g.ref, g.inv, g.base, g.coef);
+                if (a.stats) *reinterpret_cast<float4*>(a.stats + 4 * n) = make_float4(g.top, g.inv, g.rest, g.coef);
             }
         }
     }
@@ -788,7 +813,7 @@ __global__ void __launch_bounds__(kThreads) k_distill_long(DistillArgs a)
         const RowGrad g = row_grad(a, l, rest, all, k2);
         if (lane == 0) {
             a.loss[n] = w * loss;
-            if (a.stats) *reinterpret_cast<float4*>(a.stats + 4 * n) = make_float4(g.ref, g.inv, g.base, g.coef);
+            if (a.stats) *reinterpret_cast<float4*>(a.stats + 4 * n) = make_float4(g.top, g.inv, g.rest, g.coef);
         }
     }
 }
@@ -813,13 +838,14 @@ __global__ void __launch_bounds__(kThreads) k_distill_grad(DistillArgs a, int bl
     IO* d = static_cast<IO*>(a.dlogits) + n * a.ds + v0;
     const float4 st = *reinterpret_cast<const float4*>(a.stats + 4 * n);
     const float w = (a.weight ? a.weight[n] : 1.0f) * (a.dloss ? a.dloss[n] : 1.0f) * a.inv_tau;
-    const float k2 = a.inv_tau * kLog2e, base = st.z, coef = w * st.w;
+    const float k2 = a.inv_tau * kLog2e, coef = w * st.w;
+    const Scale c = scale_of(st.z, k2);
     const bool live = !(w == 0.0f) && !(st.y == 0.0f);
     const int phase = (int)phase_of(z, sizeof(IO));
     const bool aligned = phase_of(d, sizeof(IO)) == (uint32_t)phase;
     const int head = aligned ? min(len, (E - phase) % E) : len, nvec = (len - head) / E;
-    const float2 kk = both(k2), mb = both(-base), cc = both(coef);
-    auto grad = [&](IO v) { return live ? from_f32<IO>(coef * fast_exp2(fmaf(to_f32(v), k2, -base))) : from_f32<IO>(0.0f); };
+    const float2 kk = both(c.k), mc = both(-c.c), cc = both(coef);
+    auto grad = [&](IO v) { return live ? from_f32<IO>(coef * fast_exp2(fmaf(to_f32(v), c.k, -c.c))) : from_f32<IO>(0.0f); };
 
     if (live) {
         // the student's logits on the list, before anything is written: dlogits may be logits
@@ -836,7 +862,7 @@ __global__ void __launch_bounds__(kThreads) k_distill_grad(DistillArgs a, int bl
         for (int q = 0; q < kVecs; ++q) {
             if (k + q * kThreads >= nvec) continue;
             if (live) {
-                grad_vector(v[q], kk, mb, cc);
+                grad_vector(v[q], kk, mc, cc);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[q].v[e] = from_f32<IO>(0.0f);
@@ -848,9 +874,10 @@ __global__ void __launch_bounds__(kThreads) k_distill_grad(DistillArgs a, int bl
     for (int k = head + nvec * E + tid; k < len; k += kThreads) d[k] = grad(z[k]);
     if (!live) return;
     __syncthreads();
+    const Scale top = scale_of(st.x, k2);
     for (int j = tid; j < a.K; j += kThreads) {
         const int64_t k = t.first[j] - v0;
-        if (t.first[j] >= 0 && k >= 0 && k < len) d[k] = from_f32<IO>(w * (fast_exp2(fmaf(t.z[j], k2, -st.x)) * st.y - t.total[j]));
+        if (t.first[j] >= 0 && k >= 0 && k < len) d[k] = from_f32<IO>(w * (fast_exp2(fmaf(t.z[j], top.k, -top.c)) * st.y - t.total[j]));
     }
 }
 

@@ -433,10 +433,11 @@ int ob_gated_scan_read_status(const void *ws, unsigned *status, void *stream);
  *   top_lse [N]:   p_j = exp(top_j/temperature - top_lse), top_lse being the teacher's
  *                  log-sum-exp of all its logits / temperature; the tokens outside the list
  *                  form one more entry with p_rest = max(0, 1 - sum p_j) and q_rest the
- *                  student's mass there (summed directly, not as 1 - sum q_j). Where q_rest
- *                  is 0 (no token is outside, or all those are at -infinity) the loss is
- *                  infinite, but a p_rest of up to 2^-24*(4*|top_lse| + K/32 + 16) is the
- *                  rounding of sum p_j there and taken as 0
+ *                  student's mass there (summed directly, not as 1 - sum q_j). Where that is
+ *                  0 (no token is outside, or all those are at -infinity) the loss is infinite,
+ *                  but a p_rest of up to 2^-24*(4*|top_lse| + K/32 + 16) is the rounding of
+ *                  sum p_j there, and where all those are below the largest logit by more
+ *                  than float32's range, exp(-87), and taken as 0
  * Terms with p = 0 are 0; a token listed twice counts with the sum of its entries. A row whose
  * weight is 0, or (without top_lse) with no entry above -infinity, has loss 0 and gradient 0,
  * whatever its logits are. weight [N] (NULL: 1) multiplies the loss.

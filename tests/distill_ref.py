@@ -2,8 +2,8 @@
 
 Plain torch in double precision on the CPU, from the formulas in include/ob.h: the gradient is
 the loss's derivative also where the listed mass S = sum p exceeds 1 (p_rest is 0 there, and the
-student's q counts S times), and where the student has no mass outside the list a p_rest within a sum's
-rounding is 0.
+student's q counts S times), and where the student has no mass that float32 shows outside the list a p_rest
+within a sum's rounding is 0.
 
 Logits are taken relative to their row's largest, dz <= 0, which leaves q and the loss as they
 are. EPS is float32's unit roundoff. An exponent dz is formed with at most 4 roundings of its own
@@ -11,6 +11,8 @@ size; a log-sum-exp has those of its terms, weighted with their shares, and C = 
 exponentials, the sum and the logarithm. p = exp(t - lse) has the roundings of t and lse, at most
 4 EPS of either, and C. Products and sums of these take C of the terms' sizes.
 """
+import math
+
 import torch
 
 from student_ref import C, EPS, HALF_ULP, TINY
@@ -76,7 +78,7 @@ def distill(logits, index, top, top_lse=None, temperature=1.0, weight=None, dlos
         rest = torch.zeros((), dtype=torch.float64)
         if top_lse is not None:
             rest = torch.clamp(1 - mass, min=0)
-            if lrest == -INF and rest <= rest_slack(float(tl), K):
+            if float(outside.max()) < -126 * math.log(2) and rest <= rest_slack(float(tl), K):
                 rest = torch.zeros_like(rest)
             lqr = lrest - lse
             if rest > 0:

@@ -34,7 +34,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct Teacher {
     int* token;     // its token (-1: padding)
     int* first;     // the token, or -1 where an earlier entry has it
-    float* t;       // its value / tau
+    float* t;       // its value
     float* total;   // p summed over the entries of one token
     float* z;       // the student's logit there
 };
@@ -152,7 +152,7 @@ __device__ __forceinline__ void put_entry(const DistillArgs& a, int64_t n, const
 {
     const int k = j < a.K ? token_at(a, n * a.K + j) : -1;
     t.token[j] = k;
-    t.t[j] = k < 0 ? -INFINITY : top_at(a, n * a.K + j) * a.inv_tau;
+    t.t[j] = k < 0 ? -INFINITY : top_at(a, n * a.K + j);
     t.z[j] = k < 0 ? -INFINITY : to_f32(z[k]);
 }
 
@@ -166,7 +166,7 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
 {
     const int lane = threadIdx.x & 31, K = a.K;
     const float k2 = a.inv_tau * kLog2e;
-    float top = -INFINITY, m = -INFINITY, lse;
+    float top = -INFINITY, m = -INFINITY, off, lse;      // log p = (t - off)/tau - lse
     for (int w = lane; w < kSeenWords; w += 32) seen[w] = 0u;
     for (int j = lane; j < K; j += 32) {
         top = fmaxf(top, t.t[j]);
@@ -175,19 +175,21 @@ __device__ List prepare_list(const DistillArgs& a, float top_lse, const Teacher&
     __syncwarp();
     m = warp_max(m);
     if (a.top_lse) {
+        off = 0.0f;
         lse = top_lse;
     } else {
-        top = warp_max(top);
+        // relative to the largest, so that neither the size of the values nor 1/tau costs precision or overflows
+        off = warp_max(top);
         float sum = 0.0f;
-        for (int j = lane; j < K; j += 32) sum += t.t[j] == -INFINITY ? 0.0f : expf(t.t[j] - top);
-        lse = top + logf(warp_sum(sum));
+        for (int j = lane; j < K; j += 32) sum += t.t[j] == -INFINITY ? 0.0f : expf((t.t[j] - off) * a.inv_tau);
+        lse = logf(warp_sum(sum));
     }
     List l{0.0f, 0.0f, 0.0f, 0.0f, m, 0.0f};
     for (int j0 = 0; j0 < K; j0 += 32) {
         const int j = j0 + lane, k = j < K ? t.token[j] : -1;
         bool taken = false;
         if (j < K) {
-            const float lp = t.t[j] - lse, p = t.t[j] == -INFINITY ? 0.0f : expf(lp);
+            const float lp = fmaf(t.t[j] - off, a.inv_tau, -lse), p = t.t[j] == -INFINITY ? 0.0f : expf(lp);
             l.mass += p;
             if (!(p == 0.0f)) l.self += p * lp;
             t.total[j] = p;
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
                 const int j = lane + 32 * q;
                 if (j >= padded(a.K)) continue;
                 t.token[j] = token[q];
-                t.t[j] = token[q] < 0 ? -INFINITY : top[q] * a.inv_tau;
+                t.t[j] = token[q] < 0 ? -INFINITY : top[q];
                 t.z[j] = logit[q];
             }
             for (int j = lane + 32 * kAhead; j < padded(a.K); j += 32) put_entry(a, n, row_of(n), t, j);

@@ -1,8 +1,10 @@
 """The distillation loss on the GPU on rows of huge or of the types' lowest values: a constant
-added to a row of logits changes nothing."""
+added to a row of logits, or to a teacher's list, changes nothing."""
 import pytest
 import torch
 
+import distill_ref as D
+import student_ref as R
 from test_gpu_distill_mass import all_ways, ops  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +76,24 @@ def test_huge_but_distinct_logits(ops, V, dtype):  # noqa: F811
     for n, scale in enumerate((1e7, 1e9, 1e11, 1e15, 1e25, 1e35)):
         k["logits"][n] = (scale * torch.randn(V, generator=g, device="cuda")).to(dtype)
     all_ways(ops, k)
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0, 3.0])
+@pytest.mark.parametrize("top_dtype", [F32, F16, BF16])
+def test_teachers_at_one_value(ops, tau, top_dtype):  # noqa: F811
+    """A teacher's list at any one value, its type's lowest too, is the uniform distribution."""
+    k = inputs(5, 3000, 6, F32, False, tau)
+    k["logits"] = torch.randn(5, 3000, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    k["top"] = torch.zeros(5, 6, dtype=top_dtype, device="cuda")
+    flat = ops.distill_loss_grad(**k)
+    lowest = torch.finfo(top_dtype).min
+    for n, value in enumerate((lowest, -lowest, lowest / 2, 5.0, -0.1)):
+        k["top"][n] = value
+    loss, d = all_ways(ops, k)
+    assert torch.equal(loss, flat[0]) and torch.equal(d, flat[1])
+    k["top"][:, 3:] = -INF
+    all_ways(ops, k)
+    k["top"][:, :2] = lowest                # one entry far above the others
+    k["top"][:, 2] = 0.0
+    loss, _ = all_ways(ops, k)
+    R.check(loss, D.distill(k["logits"], k["index"][:, 2:3], k["top"][:, 2:3], temperature=tau)["loss"])

@@ -17,6 +17,7 @@ import functools
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import ob
 
@@ -208,6 +209,7 @@ def gated_scan_step(x, r, i, decay, h, reset=None):
     y = torch.empty((B, D), dtype=x.dtype, device=x.device)
     _call(x.device, "ob_gated_scan_step", B, D, ob.DTYPES[x.dtype], x.data_ptr(), x.stride(0), r.data_ptr(),
           r.stride(0), i.data_ptr(), i.stride(0), decay.data_ptr(), ob._ptr(reset), h.data_ptr(), y.data_ptr())
+    increment_version(h)
     return y
 
 
@@ -310,11 +312,13 @@ def distill_loss_grad(logits, index, top, top_lse=None, temperature=1.0, weight=
     put what the loss is scaled by (1 / tokens, a loss scale, 0 for padding) into ``weight``
     and call ``logits.backward(dlogits)``. Returns (loss [...], dlogits [..., V] in the type
     of logits). ``out`` receives dlogits; it may be ``logits`` itself where nothing reads
-    those again, and must not overlap them otherwise."""
+    those again (autograd raises where an operation has saved them for its backward pass), and
+    must not overlap them otherwise."""
     _need_data(logits, "logits")
     flat, index, top, top_lse, temperature, weight = _distill_inputs(logits.detach(), index, top, top_lse, temperature,
                                                                      weight)
-    if out is None:
+    given = out
+    if given is None:
         d = torch.empty(flat.shape, dtype=flat.dtype, device=flat.device)
         out = d if logits.dim() == 2 else d.view(logits.shape)
     else:
@@ -329,4 +333,6 @@ def distill_loss_grad(logits, index, top, top_lse=None, temperature=1.0, weight=
         except RuntimeError:
             raise ValueError("out must have rows at one stride") from None
     loss = _distill_forward(_distill_args(flat, index, top, top_lse, temperature, weight), flat, d, None)
+    if given is not None:
+        increment_version(given)
     return loss if logits.dim() == 2 else loss.view(logits.shape[:-1]), out

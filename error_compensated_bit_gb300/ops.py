@@ -295,11 +295,13 @@ def distill_loss(logits, index, top, top_lse=None, temperature=1.0, weight=None)
     one more entry, with the mass that both sides have left there (a student without any has an
     infinite loss, unless the teacher's is within rounding of 0). ``weight`` [...] float32
     multiplies the loss; rows of weight 0 (padding) and, without ``top_lse``, rows without an
-    entry give 0. Differentiable by logits. Reduce it as the training loop wants; where the
-    gradient's row factors are known beforehand, ``distill_loss_grad`` reads the logits once
-    instead of twice.
+    entry give 0. Differentiable by logits alone: the others must not require a gradient.
+    Reduce it as the training loop wants; where the gradient's row factors are known
+    beforehand, ``distill_loss_grad`` reads the logits once instead of twice.
     """
     flat, index, top, top_lse, temperature, weight = _distill_inputs(logits, index, top, top_lse, temperature, weight)
+    if _differentiates(top, top_lse, weight):
+        raise ValueError("distill_loss is differentiable by logits alone: detach top, top_lse and weight")
     if torch.is_grad_enabled() and flat.requires_grad:
         loss = _Distill.apply(flat, index, top, top_lse, temperature, weight)
     else:

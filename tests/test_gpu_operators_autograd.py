@@ -1,5 +1,5 @@
-"""The operators within torch: tensors that they write tell autograd so, and passes are captured in
-graphs."""
+"""The operators within torch: tensors that they write tell autograd so, arguments that get no
+gradient are refused when they ask for one, and passes are captured in graphs."""
 import pytest
 import torch
 
@@ -58,6 +58,19 @@ def test_a_gradient_over_the_logits_raises_their_version(ops):  # noqa: F811
         zi = z.clone()
         ops.distill_loss_grad(zi, index, top, out=zi)
     assert torch.isfinite(zi).all()
+
+
+def test_a_teacher_that_asks_for_a_gradient_is_refused(ops):  # noqa: F811
+    z, index, top = loss_inputs()
+    z.requires_grad_(True)
+    ones = torch.ones(6, device="cuda")
+    for bad in (dict(top=top.clone().requires_grad_(True)), dict(top=top, weight=ones.clone().requires_grad_(True)),
+                dict(top=top, top_lse=ones.clone().requires_grad_(True))):
+        with pytest.raises(ValueError, match="detach"):
+            ops.distill_loss(z, index, **bad)
+        with torch.no_grad():
+            ops.distill_loss(z, index, **bad)
+        ops.distill_loss_grad(z, index, **bad)      # returns the gradient by the logits, and says so
 
 
 def capture(run):

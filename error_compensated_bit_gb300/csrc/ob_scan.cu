@@ -660,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_bwd(ScanArgs p, floa
 
         // from the last step to the first: g = dy + flow, and every gradient from it
         float2 sum = both(0.0f);
-        const float2 minus_d = make_float2(d.x * -kTwoM32, d.y * -kTwoM32), one = hold(1.0f), minus_one = hold(-1.0f),
-                     minus_m32 = hold(-kTwoM32);
+        // dr's factor 2^-32 goes with 1 - s(r): decays below 2^-94 would lose bits to it
+        const float2 minus_d = make_float2(-d.x, -d.y), one = hold(1.0f), minus_one = hold(-1.0f),
+                     minus_m32 = hold(-kTwoM32), m32 = hold(kTwoM32), minus_m64 = hold(-kTwoM32 * kTwoM32);
         const int64_t o = ((int64_t)q.b * p.T + t0) * p.D + q.col;
         const int rows = here ? max(0, min(L, (int)p.T - t0)) : 0;
         const int64_t back = -p.D * (int64_t)sizeof(IO);
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_bwd(ScanArgs p, floa
                 const float2 inner = fma2(mul2(ax, rb), minus_one, mul2(keep, u[m]));
                 const float2 dlog = mul2(mul2(gt, inner), s32[m]);        // times 2^32 s(r)
                 const float2 gb = mul2(gt, b[m]);
-                const float2 one_i = fma2(si[m], minus_one, one), one_r = fma2(s32[m], minus_m32, one);
+                const float2 one_i = fma2(si[m], minus_one, one), one_r = fma2(s32[m], minus_m64, m32);
                 const float2 ox = mul2(gb, si[m]), oi = mul2(mul2(gb, xs), one_i), orr = mul2(mul2(dlog, minus_d), one_r);
                 sum = fma2(dlog, minus_m32, sum);
                 if constexpr (V == 2) {

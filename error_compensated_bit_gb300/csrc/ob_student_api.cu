@@ -224,7 +224,7 @@ int ob_distill(int64_t N, int64_t V, int64_t K, int dtype, const void* logits, i
     OB_TRY(check_distill(N, V, K, dtype, logits, index, index_bits, top, top_dtype, top_lse, weight, temperature));
     OB_TRY(want(loss, 4));
     OB_TRY(may(dlogits, dtype_bytes(dtype)));
-    if (dlogits == logits && ds != zs) return OB_EINVAL;
+    if (dlogits == logits && N > 1 && ds != zs) return OB_EINVAL;
     if (dlogits && N > 1 && (ds < 0 ? -ds : ds) < V) return OB_EINVAL;
     OB_TRY(may(stats, 16));
     if (dlogits && distill_workspace_bytes(N, V, dtype)) OB_TRY(want(ws, 256));
@@ -244,7 +244,7 @@ int ob_distill_bwd(int64_t N, int64_t V, int64_t K, int dtype, const void* logit
     OB_TRY(want(stats, 16));
     OB_TRY(want(dloss, 4));
     OB_TRY(want(dlogits, dtype_bytes(dtype)));
-    if (dlogits == logits && ds != zs) return OB_EINVAL;
+    if (dlogits == logits && N > 1 && ds != zs) return OB_EINVAL;
     if (N > 1 && (ds < 0 ? -ds : ds) < V) return OB_EINVAL;
     DistillArgs a{N, V, (int)K, dtype, index_bits, top_dtype, logits, zs, index, top, top_lse, weight, dloss,
                   1.0f / temperature, nullptr, dlogits, ds, const_cast<float*>(stats)};

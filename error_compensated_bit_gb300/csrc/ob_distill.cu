@@ -5,18 +5,19 @@
 //   sum_j p_j log p_j - sum_j p_j (z'_j - lse)  [+ p_rest (log p_rest - (rest - lse))]
 // and its gradient by z, times tau, with M = sum_j p_j + p_rest:
 //   M q_v - p_v on the list, softmax_rest(z')_v * (M q_rest - p_rest) outside it,
-// q_rest = exp(rest - lse), p_rest = 0 without a rest entry. M is 1 unless the list's own mass is
-// above 1 (top values rounded to 16 bits beside the log-sum-exp of the unrounded ones): p_rest is 0 there. Summing the rest apart (rather
-// than as 1 minus the list) keeps its precision when the list holds nearly all the mass.
+// q_rest = exp(rest - lse), p_rest = 0 without a rest entry. M is 1 unless the list's own mass is above
+// 1 (top values rounded to 16 bits beside the log-sum-exp of the unrounded ones): p_rest is 0 there.
+// Summing the rest apart (rather than as 1 minus the list) keeps its precision when the list holds
+// nearly all the mass.
 //
 // What has to move: each logit in once and, with the gradient, out once; the lists are small. The
 // one pass keeps a row on chip (k_distill_row), so nothing is read twice. What bounds it is the
 // chain of a row, copy, maximum, sum, the blocks' exchange, gradient, of which three run in turn on
-// an SM, at 58% of the issue slots; DRAM runs at two thirds of its rate. Measured (CUDA events),
-// loss with gradient: 8192 x 32000 bfloat16, K = 64, 199 us (5.3 TB/s); 8192 x 131072, K = 100, with
-// the rest entry, 890 us (4.8 TB/s); 4096 x 50257 float32, K = 20, 332 us (5.0 TB/s). The loss
-// alone: 128, 544 and 222 us (3.7 - 4.1 TB/s). Backward from saved statistics: 198, 722 and 287 us
-// (5.3 - 6.0 TB/s).
+// an SM, at 60% of the issue slots and 68% of DRAM's rate (the loss alone 53 and 54%). Measured (CUDA
+// events), loss with gradient: 8192 x 32000 bfloat16, K = 64, 192 us (5.5 TB/s); 8192 x 131072, K = 100,
+// with the rest entry, 845 us (5.1 TB/s); 4096 x 50257 float32, K = 20, 327 us (5.0 TB/s). The loss
+// alone: 125, 542 and 216 us (3.8 - 4.2 TB/s). Backward from saved statistics: 174, 692 and 254 us
+// (6.0 - 6.5 TB/s).
 #include <algorithm>
 
 #include "ob_student.cuh"
@@ -548,9 +549,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) k_distill_row(DistillArgs a,
 
     if (warp == kWarps) {
         // the first kAhead entries a lane of the next row's list are on their way while this row's are
-        // prepared: first their tokens and values, then the student's logits there (without branches:
-        // with the loads of lists shorter than 128 branched around, 8192 x 131072 took 1,047 us
-        // instead of 892)
+        // prepared: first their tokens and values, then the student's logits there
         constexpr int kAhead = 4;
         int token[kAhead];
         float top[kAhead], logit[kAhead], lse = 0.0f;
@@ -885,9 +884,9 @@ __global__ void __launch_bounds__(kThreads) k_distill_grad(DistillArgs a, int bl
 
 // How a row is shared out: the fewest blocks whose slices are at most kSliceWant bytes, so that three
 // of them fit an SM and one row's copy overlaps another's arithmetic and stores (8192 x 32000
-// bfloat16: 201 us with slices of 64 KB, 311 us with 32 KB; 8192 x 131072: 890 and 1,391 us); more
-// while the launch would leave SMs without a block (4 x 32000 float32: 7.5 us with eight blocks a row,
-// 8.8 us with two); larger slices when eight blocks are not enough.
+// bfloat16: 192 us with slices of 64 KB, 270 us with 32 KB; 8192 x 131072: 848 and 1,332 us); more
+// while the launch would leave SMs without a block (4 x 32000 float32: 7.8 us with eight blocks a row,
+// 9.0 us with two); larger slices when eight blocks are not enough.
 constexpr int kSliceWant = 65536 + 1024, kSliceMost = 188416;
 constexpr size_t kSmemMost = 231424;    // of a block, beside its static part
 

@@ -8,13 +8,14 @@
 // block through shared memory and along time by look-back (ob_scan.cuh), each element being gated
 // once and kept in registers until the state that reaches its tile is known.
 //
-// What bounds them now is issue slots, then memory: a pair of 16-bit elements takes 93 instructions
-// forward and some 180 backward (ncu, 8 x 2048 x 2048 bfloat16), where the measured 6.7 TB/s would
-// feed a pair every 89 and 156 clocks of an SM quarter, and with 16 warps an SM 56% of the slots are
-// used. Hence the packed arithmetic and everything else here that saves instructions. Measured on
-// bfloat16 without resets (CUDA events, launches back to back):
-//   forward   8 x 2048 x 2048    86 us, 3.1 TB/s;   16 x 4096 x 4096   514 us, 4.2 TB/s
-//   backward  8 x 2048 x 2048   177 us, 2.7 TB/s;   16 x 4096 x 4096   956 us, 3.9 TB/s
+// What bounds them now is the latency of the instructions, with too few warps to hide it: a pair of
+// 16-bit elements takes 87 instructions forward and 179 backward (ncu, 8 x 2048 x 2048 bfloat16), and
+// with 16 warps an SM (128 registers a thread) 53 and 60% of the issue slots and 38% of DRAM's rate are
+// used; a warp mostly waits for a fixed latency or for the arithmetic pipes. Hence the packed arithmetic
+// and everything else here that saves instructions. Measured on bfloat16 without resets (CUDA events,
+// launches back to back):
+//   forward   8 x 2048 x 2048    83 us, 3.2 TB/s;   16 x 4096 x 4096   505 us, 4.3 TB/s
+//   backward  8 x 2048 x 2048   162 us, 2.9 TB/s;   16 x 4096 x 4096   937 us, 4.0 TB/s
 // The smaller case has 256 chains for 304 blocks.
 #include <algorithm>
 #include <type_traits>
@@ -99,8 +100,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 // How a lane's words come into shared memory: 16 bytes at a time (a row's 128 bytes by eight
 // lanes) where every row starts on 16 bytes and x, r and i have the same strides (their offsets are
 // then computed once), else word by word; a single 16-bit channel, narrower than any
-// asynchronous copy, through a register. 16 x 4096 x 4096 bfloat16 forward, backward: 513, 914 us
-// wide; 715, 1,035 us by words (the same tensors 4 bytes on); 937, 1,456 us by single channels (2
+// asynchronous copy, through a register. 16 x 4096 x 4096 bfloat16 forward, backward: 505, 937 us
+// wide; 723, 1,061 us by words (the same tensors 4 bytes on); 949, 1,507 us by single channels (2
 // bytes on: odd numbers of channels, odd addresses).
 enum Copy { kWide, kWord, kPlain };
 
@@ -346,7 +347,7 @@ __device__ __forceinline__ float2 state_at(const ScanArgs& p, const Place& q, co
 }
 
 // kReset: there are reset flags. Without, what follows from them is left out (backward, 16 x 4096 x
-// 4096 bfloat16 956 instead of 1,031 us).
+// 4096 bfloat16 937 us where the kernel with them takes 1,016).
 template <typename IO, int V, int L, Copy kCopy, bool kReset>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_fwd(ScanArgs p, Grid g)
 {
@@ -451,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_fwd(ScanArgs p, Grid
             }
         }
         // what the next tile of the chain waits for goes out before the copies of this block's next start
-        // (65536 x 768 float32 228 instead of 242 us), but for two channels a lane, where it costs
-        // registers that spill
+        // (65536 x 768 float32 217 instead of 231 us); with two channels a lane the orders are within 2% of
+        // each other (16 x 4096 x 4096 bfloat16 forward 495 so and 505, backward 947 and 937 us)
         constexpr bool kEarly = V == 1;
         float2 h;
         auto hand_on = [&] {
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_bwd(ScanArgs p, floa
             a[m] = e.a, s32[m] = e.s32, si[m] = e.si, b[m] = e.b;
             u[m] = mul2(mul2(e.b, e.si), pair_at<IO, V>(wx, m));
             // one pair after the other: more of them under way at a time spill (16 x 4096 x 4096 bfloat16
-            // with resets 1,031 instead of 1,240 us, without 956 instead of 970)
+            // with resets 1,016 instead of 1,195 us, without 937 instead of 943)
             if (V == 2) asm volatile("" : "+f"(a[m].x), "+f"(a[m].y), "+f"(u[m].x), "+f"(u[m].y));
         }
         sh[turn][warp][lane] = resets ? end_state<V, L, true>(a, u, both(0.0f), resets)
@@ -757,8 +758,8 @@ __global__ void __launch_bounds__(256) k_column_sums(const float* part, int64_t 
 }
 
 // One token for B sequences; two channels a thread where V is 2 (an even number of channels). One
-// sequence of 2,048 channels takes the 1.8 us of an empty launch in a graph; 512 of 4,096, 33.6 MB,
-// 7.7 us, from the L2 in part.
+// sequence of 2,048 channels takes 2.0 us in a graph, an empty launch 1.8; 512 of 4,096, 33.6 MB,
+// 8.0 us, from the L2 in part.
 template <typename IO, int V>
 __global__ void __launch_bounds__(128) k_scan_step(ScanStepArgs p, int64_t ncols)
 {
@@ -827,11 +828,13 @@ bool alike(const ScanArgs& a)
 
 // One wave of persistent blocks. Where there are at least as many chains as blocks, a block takes up to
 // 8 consecutive tiles of a chain (at least 6 items a block are left, for balance): 16 x 4096 x 4096
-// bfloat16 forward, backward 515, 962 us instead of 568, 1,078 us with one tile each; 32 x 512 x 2048
-// 84, 176 instead of 87, 182 us. With nearly as many, each block takes a whole chain and none waits:
-// 8 x 2048 x 2048 (256 chains for 304 blocks) 85, 181 us instead of 99, 196; the blocks left idle
-// would outweigh that from about 0.78 of their number down. With fewer, an item would keep its
-// successor's block waiting, so each is one tile.
+// bfloat16 forward, backward 505, 937 us instead of 540, 1,027 us with one tile each; 64 x 512 x 4096
+// 270, 510 instead of 276, 539 us. With nearly as many, each block takes a whole chain and none waits:
+// B x 2048 x D bfloat16 with 256 chains for 304 blocks 83, 163 us instead of 92, 178, with 288 (4,096
+// steps) 159, 307 instead of 188, 351; with 240 83, 163 instead of 89, 171, with 224 82, 162 instead of 86, 162,
+// with 208 82, 163 instead of 82, 156: below about 0.72 of the blocks' number the idle ones outweigh it, and 0.8
+// is a little above that. With fewer, an item would keep its successor's block waiting, so each is one
+// tile.
 template <int V, int L, auto kKernel, typename... A>
 cudaError_t launch_tiles(const ScanArgs& a, int tensors, cudaStream_t s, A... more)
 {

@@ -97,7 +97,7 @@ struct DistillArgs {
     float* loss;                  // [N]
     void* dlogits;                // [N][V] or null
     int64_t ds;                   // row stride of dlogits
-    float* stats;                 // [N][4] or null: see RowGrad in ob_distill.cu, and 1 (0: no loss)
+    float* stats;                 // [N][4] or null: RowGrad in ob_distill.cu (inv 0: no loss)
 };
 
 size_t scan_workspace_bytes(int64_t B, int64_t T, int64_t D, int dtype, int backward);

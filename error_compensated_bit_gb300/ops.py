@@ -181,12 +181,13 @@ def gated_scan(x, r, i, decay, h0=None, reset=None):
         a_t = exp(-decay * s(r_t))
         h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * s(i_t) * x_t
 
-    ``decay`` [D] float32, >= 0, is the rate at an open gate; ``h0`` [B, D] float32 the state
-    before the first token (None: zero); ``reset`` [B, T] bool marks tokens that start a
-    sequence, before which the state is dropped. Returns y [B, T, D] in the type of x and the
-    last state [B, D] in float32. Differentiable by x, r, i, decay and h0; the state is
-    float32 throughout, in the backward pass too. Batch and time strides are free (slices of
-    a joint projection need no copy); channels that are not adjacent are copied first.
+    ``decay`` [D] float32, from 0 to 1e28 (not checked; a negative one gives NaN), is the rate
+    at an open gate; ``h0`` [B, D] float32 the state before the first token (None: zero);
+    ``reset`` [B, T] bool marks tokens that start a sequence, before which the state is
+    dropped, whatever it is. Returns y [B, T, D] in the type of x and the last state [B, D]
+    in float32. Differentiable by x, r, i, decay and h0; the state is float32 throughout, in
+    the backward pass too. Batch and time strides are free (slices of a joint projection need
+    no copy); channels that are not adjacent are copied first.
     """
     x, r, i, decay, reset = _scan_inputs(x, r, i, decay, reset, 3)
     h0 = _need(h0, "h0", (x.shape[0], x.shape[2]), torch.float32, x.device)

@@ -372,7 +372,8 @@ typedef struct ob_view {
  *   a_t = exp(-decay[d]*s(r_t));
  *   h_t = a_t*h_{t-1} + sqrt(1 - a_t^2)*s(i_t)*x_t;      y_t = h_t
  * where h_{-1} is h0[b][d] (0 when h0 is NULL) and h_{t-1} is replaced by 0 where
- * reset[b][t] is non-zero (the first token of a packed sequence; NULL: none).
+ * reset[b][t] is non-zero (the first token of a packed sequence; NULL: none). Infinities and
+ * NaN stay in their sequence, and in it go on to its end (backward to its start).
  * decay [D] must lie in [0, 1e28] (a negative one gives NaN); 1 - a^2 is formed without
  * cancellation for a near 1. y [B][T][D] and h_last [B][D] (the state after the last token;
  * h0 when T is 0; may be NULL) are written. states, when not NULL, receives what the
